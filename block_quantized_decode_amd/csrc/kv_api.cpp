@@ -157,7 +157,10 @@ int kv_attention(const qbd_kv_cache* cache, const void* q, int dtype, int64_t q_
     if (!q || !out || !lens || (table_width > 0 && !table)) return QBD_ERR_NULL;
     if ((st = check_rows(T, qheads, kv.dim, q_token_stride, q_head_stride, eb)) != QBD_OK) return st;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(q_starts, 4)) return QBD_ERR_ALIGN;
-    const int64_t need = qbd::kv_plan::work_bytes(kv.dim, kv.heads, static_cast<int>(qheads), batch, T, max_q, max_len);
+    // the size that was asked for, or what this launch takes should that be more
+    const int64_t asked = qbd::kv_plan::work_bytes(kv.dim, kv.heads, static_cast<int>(qheads), batch, T, max_q, max_len);
+    const int64_t taken = qbd::kv_plan::work_bytes(kv.dim, kv.heads, static_cast<int>(qheads), batch, T, max_q, max_len, window);
+    const int64_t need = taken > asked ? taken : asked;
     if (need > 0) {
         if (!work || work_bytes < need) return QBD_ERR_WORK;
         if (!aligned(work, 256)) return QBD_ERR_ALIGN;

@@ -129,7 +129,9 @@ QBD_HD constexpr int prompt_groups_a_cu(int nb, int waves) {
 // so it takes over where rows x heads x (keys + 1300) pass 40 million, and
 // near that for the other sizes and codes (256 elements, 2048 keys: 1024 x 8
 // 73 / 69; 64 elements, 8-bit, 8192 keys: 512 x 8 39 / 42).  A length that the
-// host does not know counts as 16384 keys, a window as its keys and the rows'.
+// host does not know counts as 16384 keys; a window as its keys and the rows',
+// but never as more than the length would without it, so that the workspace,
+// whose size is asked without the window, holds whatever it chooses.
 constexpr int kPromptRows = 96;
 constexpr double kPromptWork = 40e6;
 constexpr int64_t kPromptKeys = 32768;  // longer counts as this
@@ -138,8 +140,8 @@ constexpr int kPromptPart = 512;  // keys of a part, at least
 constexpr PromptPlan prompt_plan(int dim, int heads, int qheads, int64_t batch, int64_t T, int64_t max_q, int64_t max_len,
                                  int64_t window) {
     const int64_t rows = most_rows(qheads / heads, T, max_q);
-    const int64_t known = most_keys(T, max_q, max_len, window);
-    const int64_t keys = known == 0 ? kPromptKeys / 2 : known < kPromptKeys ? known : kPromptKeys;
+    const int64_t known = most_keys(T, max_q, max_len, window), most_counted = max_len > 0 ? kPromptKeys : kPromptKeys / 2;
+    const int64_t keys = known == 0 || known > most_counted ? most_counted : known;
     if (rows < kPromptRows || static_cast<double>(rows) * heads * batch * (keys + 1300) < kPromptWork) return PromptPlan{0, 0, 1};
     const int take = (dim == 64 || dim == 128) && rows > 128 ? 256 : 128;
     const int64_t tiles = (rows + take - 1) / take, fill = 256 * prompt_groups_a_cu(dim / 32, take / 32);
@@ -150,15 +152,18 @@ constexpr PromptPlan prompt_plan(int dim, int heads, int qheads, int64_t batch, 
     return PromptPlan{take, tiles, static_cast<int>(parts)};
 }
 
-// Partial results: for each part of a prompt's rows (a window never makes
-// more of them), or for each workgroup of the split kernel two slots (the item
-// that its share cuts at the start, and the one it cuts at the end) of 16 * RT
-// rows: dim sums, a reference and a weight total a row, a note of each item.
-constexpr int64_t work_bytes(int dim, int heads, int qheads, int64_t batch, int64_t T, int64_t max_q, int64_t max_len) {
-    const PromptPlan plan = prompt_plan(dim, heads, qheads, batch, T, max_q, max_len, 0);
+// Partial results: for each part of a prompt's rows, or for each workgroup of
+// the split kernel two slots (the item that its share cuts at the start, and
+// the one it cuts at the end) of 16 * RT rows: dim sums, a reference and a
+// weight total a row, a note of each item.  The size is asked for without a
+// window (0), under which a call never takes more: fewer keys make neither
+// more parts nor a second launch.
+constexpr int64_t work_bytes(int dim, int heads, int qheads, int64_t batch, int64_t T, int64_t max_q, int64_t max_len,
+                             int64_t window = 0) {
+    const PromptPlan plan = prompt_plan(dim, heads, qheads, batch, T, max_q, max_len, window);
     const int64_t prompt = plan.parts > 1 ? plan.row_tiles * plan.parts * heads * batch * plan.rows * (dim + 2) * 4 : 0;
     const int64_t rows = 16 * kRowTiles;
-    const bool once = direct(dim, max_len, split_items(heads, qheads, batch, T, max_q), batch);
+    const bool once = direct(dim, most_keys(T, max_q, max_len, window), split_items(heads, qheads, batch, T, max_q), batch);
     const int64_t split = once ? 0 : 2 * kMaxSplitGroups * (rows * (dim + 2) * 4 + 32);
     return prompt > split ? prompt : split;
 }
