@@ -148,6 +148,7 @@ int kv_attention(const qbd_kv_cache* cache, const void* q, int dtype, int64_t q_
     if (table_width < 0 || table_width > kMaxDim || max_q < 0 || max_len < 0 || window < 0 || work_bytes < 0) return QBD_ERR_SHAPE;
     if (table_width > kMaxDim >> kv.page_shift) return QBD_ERR_SHAPE;  // positions are 32-bit
     if (batch > 0 && table_width > kMaxPlane / 4 / batch) return QBD_ERR_SHAPE;
+    if (window > int64_t{1} << 31) window = int64_t{1} << 31;  // positions lie below it: the kernels subtract a window from them
     if ((window > 0 && !causal) || !std::isfinite(scale)) return QBD_ERR_SHAPE;
     if (T > 0 && qheads * kv.dim > kMaxPlane / 4 / T) return QBD_ERR_SHAPE;
     if (T > 0 && (batch == 0 || (!q_starts && T % batch != 0))) return QBD_ERR_SHAPE;

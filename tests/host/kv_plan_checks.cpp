@@ -103,11 +103,28 @@ void check_window_workspace() {
     g_failures += bad + (in_parts == 0);
 }
 
+// A row's window is found as position - window in 64 bits, for rows as far
+// before the first key as a call's sizes allow.
+void check_window_range() {
+    for (int64_t window : {int64_t{1} << 31, int64_t{1} << 62, INT64_MAX - (int64_t{1} << 31), INT64_MAX - 1, INT64_MAX}) {
+        int64_t need = 0;
+        if (attend({64, 2, 4, 1, 100, 0, 5000, window}, need) != QBD_OK) ++g_failures;
+        const int64_t lowest = int64_t{0} - ((int64_t{1} << 31) - (int64_t{1} << 20));
+        int64_t first = 0;
+        if (__builtin_sub_overflow(lowest, g_attn.window, &first)) {
+            std::fprintf(stderr, "window %lld reaches the kernels as %lld\n", (long long)window, (long long)g_attn.window);
+            ++g_failures;
+        }
+        if (g_attn.window < int64_t{1} << 31) ++g_failures;  // no position is out of it
+    }
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
     const char* which = argc > 1 ? argv[1] : "";
     if (!std::strcmp(which, "window_workspace")) check_window_workspace();
+    else if (!std::strcmp(which, "window_range")) check_window_range();
     else return 2;
     if (g_failures) return 1;
     std::printf("%s passed\n", which);

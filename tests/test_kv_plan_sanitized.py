@@ -32,3 +32,7 @@ def checks(tmp_path_factory):
 
 def test_window_never_takes_more_than_the_workspace_asked_for(checks):
     checks("window_workspace")
+
+
+def test_windows_near_the_types_limit_reach_the_kernels_in_range(checks):
+    checks("window_range")
