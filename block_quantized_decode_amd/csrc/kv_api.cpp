@@ -151,6 +151,7 @@ int kv_attention(const qbd_kv_cache* cache, const void* q, int dtype, int64_t q_
     if (window > int64_t{1} << 31) window = int64_t{1} << 31;  // positions lie below it: the kernels subtract a window from them
     if ((window > 0 && !causal) || !std::isfinite(scale)) return QBD_ERR_SHAPE;
     if (T > 0 && qheads * kv.dim > kMaxPlane / 4 / T) return QBD_ERR_SHAPE;
+    if (T > 0 && qheads / kv.heads > kMaxDim / T) return QBD_ERR_SHAPE;  // rows of a cached head are 32-bit
     if (T > 0 && (batch == 0 || (!q_starts && T % batch != 0))) return QBD_ERR_SHAPE;
     if (T == 0) return QBD_OK;
     const auto elem = static_cast<qbd::Elem>(dtype);

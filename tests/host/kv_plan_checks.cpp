@@ -119,12 +119,30 @@ void check_window_range() {
     }
 }
 
+// The rows of one cached head (tokens times query heads of its group) are
+// counted in 32 bits.
+void check_row_count() {
+    const int64_t most = (int64_t{1} << 31) - (int64_t{1} << 20);
+    int64_t need = 0;
+    for (int64_t group : {1, 2, 64})
+        for (int64_t T : {most / group, most / group + 1, (int64_t{1} << 32) / group}) {
+            if (T > most) continue;
+            const int calls = g_calls, st = attend({64, 1, group, 1, T, 0, 5000, 0}, need);
+            const bool fits = group * T <= most;
+            if (fits != (st == QBD_OK) || (!fits && (st != QBD_ERR_SHAPE || g_calls != calls))) {
+                std::fprintf(stderr, "group %lld T %lld: status %d\n", (long long)group, (long long)T, st);
+                ++g_failures;
+            }
+        }
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
     const char* which = argc > 1 ? argv[1] : "";
     if (!std::strcmp(which, "window_workspace")) check_window_workspace();
     else if (!std::strcmp(which, "window_range")) check_window_range();
+    else if (!std::strcmp(which, "row_count")) check_row_count();
     else return 2;
     if (g_failures) return 1;
     std::printf("%s passed\n", which);

@@ -36,3 +36,7 @@ def test_window_never_takes_more_than_the_workspace_asked_for(checks):
 
 def test_windows_near_the_types_limit_reach_the_kernels_in_range(checks):
     checks("window_range")
+
+
+def test_rows_of_a_head_are_refused_where_32_bits_do_not_count_them(checks):
+    checks("row_count")
