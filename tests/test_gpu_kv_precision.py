@@ -1,0 +1,37 @@
+"""What the roundings that include/qbd.h states leave of kv_attention's results on inputs that bring them out: against the
+float64 reference, within the bound that follows from them."""
+import numpy as np
+import pytest
+import torch
+
+import block_quantized_decode_amd as qbd
+from kv_util import Cache, check_attention, device, gpu, kv, note
+from test_gpu_kv import FORMATS, layout
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("kbits,vbits", FORMATS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 9, 40])
+def test_fp32_scores_of_keys_with_an_outlier_that_the_query_compensates(new, dim, kbits, vbits):
+    """Keys whose blocks hold one large channel and nothing beside it, queries with a mean that are small in that channel:
+    the score is a sum of small terms, and the large ones of the query meet codes of zero."""
+    rng = np.random.default_rng(dim + new)
+    lens, page, heads, group = [5, 41, 60], 16, 2, 3
+    table, pages = layout(rng, page, lens)
+    cache = Cache(rng, pages, heads, page, dim, kbits, vbits)
+    top, nb = kv.LEVELS[kbits], dim // 32
+    at = np.arange(nb) * 32 + rng.integers(0, 32, size=nb)
+    cache.codes[0][:] = 0
+    cache.codes[0][..., at] = rng.choice([-top, top], size=(pages, heads, page, nb))
+    cache.scales[0][:] = rng.uniform(0.2, 0.3, size=cache.scales[0].shape)
+    cache.upload()
+    q = (40 + 20 * rng.standard_normal((3 * new, heads * group, dim))).astype(np.float32)
+    q[..., at] = rng.standard_normal((3 * new, heads * group, nb)) * 0.5 / top
+    starts = (np.arange(4) * new).astype(np.int32)
+    note("kv attention compensated outliers", new, dim, kbits, vbits)
+    ref, mass, reach = kv.attention(q.astype(np.float64), cache.k, cache.v, table, lens, starts, scale=1.0)
+    for hints in ({}, dict(max_q=new, max_len=60)):
+        out = qbd.kv_attention(gpu(q), *cache.planes, gpu(table), gpu(np.array(lens, dtype=np.int32)), q_starts=gpu(starts), scale=1.0, **hints)
+        check_attention("compensated outliers", out, ref, mass, reach, 60, "f32")
