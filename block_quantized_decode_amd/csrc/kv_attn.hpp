@@ -67,12 +67,6 @@ __device__ __forceinline__ h2 bytes_of(uint32_t w) {
     return as_h2(__builtin_amdgcn_perm(0x64646464u, w, 0x04000400u | I | J << 16)) - h2{1152.f16, 1152.f16};
 }
 
-// Bytes I and J of w as n * 2^-24.
-template <int I, int J>
-__device__ __forceinline__ h2 bytes_small(uint32_t w) {
-    return as_h2(__builtin_amdgcn_perm(w, w, 0x0c000c00u | I | J << 16));
-}
-
 // N words in the widest loads that their number allows (p is aligned to it).
 template <int N>
 __device__ __forceinline__ void load_words(uint32_t (&w)[N], const void* p) {
@@ -101,19 +95,6 @@ template <int BITS, int NB>
 struct KCodes {
     uint32_t w[NB * BITS / 4];
     __device__ __forceinline__ void load(const uint8_t* p) { load_words<NB * BITS / 4>(w, p); }
-    // the codes plus kOffset as binary16 numbers below the normal range, n *
-    // 2^-24 (the matrix cores take them as they are); in 4-bit blocks slots
-    // 4 .. 7 hold 16 n * 2^-24
-    static constexpr float kOffset = BITS == 4 ? 8.f : 128.f;
-    __device__ __forceinline__ h8 small(int b) const {
-        if constexpr (BITS == 4) {
-            const uint32_t x = w[b], y = x >> 8;
-            return as_h8(as_h2(x & 0x000f000fu), as_h2(y & 0x000f000fu), as_h2(x & 0x00f000f0u), as_h2(y & 0x00f000f0u));
-        } else {
-            const uint32_t x = w[2 * b] ^ 0x80808080u, y = w[2 * b + 1] ^ 0x80808080u;
-            return as_h8(bytes_small<0, 1>(x), bytes_small<2, 3>(x), bytes_small<0, 1>(y), bytes_small<2, 3>(y));
-        }
-    }
     __device__ __forceinline__ h8 operand(int b, uint32_t k) const {
         if constexpr (BITS == 4) {
             const uint32_t x = w[b];

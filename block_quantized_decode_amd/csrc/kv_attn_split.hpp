@@ -221,20 +221,16 @@ __device__ __forceinline__ int find_sequence(const AttnArgs& a, const Split& sp,
 
 
 // A lane's part of a query row in operand order, scaled by a power of two to
-// a maximum near 2^10.  With 16-bit rows codes enter as (code + offset) 2^-24:
-// the offset times the sum of a block's elements is where its dot starts, and
-// the high half of a 4-bit block, whose codes are 16-fold, is divided by 16.
-// With fp32 rows they enter as they are: the offset's share of the dot, which
-// cancels, is large where a block's codes are small (an outlier beside them,
-// queries with a mean), and its fp32 roundings were up to some hundred times
-// the dot's own.
+// a maximum near 2^10.  The codes that it meets are the exact ones: entered with
+// an offset (fewer instructions) they make a block's dot the difference of two
+// larger sums, whose fp32 roundings were up to some hundred times the dot's own
+// where a block's codes are small (an outlier beside them, queries with a mean).
 template <int KB, int NB, bool SPLIT>
 struct Query {
     static constexpr int kRun1 = KB == 4 ? 16 : 4;  // a slot's eight elements are two runs of four
     Run4<SPLIT> raw[NB][2];
     h8 hi[NB];
     h8 lo[SPLIT ? NB : 1];
-    f4 from[SPLIT ? 1 : NB];
     float c;  // a score in units of log2
     __device__ __forceinline__ void fetch(const AttnArgs& a, int64_t at, int g) {
         const int first = KB == 4 ? 4 * g : 8 * g;
@@ -255,24 +251,14 @@ struct Query {
         top = fmaxf(top, __shfl_xor(top, 32));
         const int e = __builtin_amdgcn_frexp_expf(top) - 10;
         const float sign = a.scale < 0.f ? -1.f : 1.f;
-        c = ldexpf(fabsf(a.scale) * 1.44269504088896340736f, SPLIT ? e : e + 24);
+        c = ldexpf(fabsf(a.scale) * 1.44269504088896340736f, e);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            float all = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float part = !SPLIT && KB == 4 && j >= 4 ? 0.0625f : 1.f;
-                const float y = part * sign * ldexpf(raw[b][j / 4].at(KB == 4 ? j % 2 * 2 + j % 4 / 2 : j % 4, a.elem), -e);
+                const float y = sign * ldexpf(raw[b][j / 4].at(KB == 4 ? j % 2 * 2 + j % 4 / 2 : j % 4, a.elem), -e);
                 hi[b][j] = static_cast<_Float16>(y);
-                const float kept = static_cast<float>(hi[b][j]);
-                if constexpr (SPLIT) lo[b][j] = static_cast<_Float16>(y - kept);
-                else all = fmaf(kept, KB == 4 && j >= 4 ? 16.f : 1.f, all);
-            }
-            if constexpr (!SPLIT) {
-                all += __shfl_xor(all, 16);
-                all += __shfl_xor(all, 32);
-                const float z = all * (-KCodes<KB, NB>::kOffset / 16777216.f);
-                from[b] = f4{z, z, z, z};
+                if constexpr (SPLIT) lo[b][j] = static_cast<_Float16>(y - static_cast<float>(hi[b][j]));
             }
         }
     }
@@ -459,14 +445,12 @@ __global__ __launch_bounds__(256, kv_plan::split_groups_a_cu(KB, VB, NB, RT)) vo
                 for (int h = 0; h < 2; ++h) {
 #pragma unroll
                     for (int y = 0; y < NB; ++y) {
-                        h8 kop;
-                        if constexpr (SPLIT) kop = k[h].operand(y, magic);
-                        else kop = k[h].small(y);
+                        const h8 kop = k[h].operand(y, magic);
 #pragma unroll
                         for (int r = 0; r < RT; ++r) {
-                            f4 d;
-                            if constexpr (SPLIT) d = mfma(kop, q[r].hi[y], mfma(kop, q[r].lo[y], f4{0.f, 0.f, 0.f, 0.f}));
-                            else d = mfma(kop, q[r].hi[y], q[r].from[y]);
+                            f4 d = {0.f, 0.f, 0.f, 0.f};
+                            if constexpr (SPLIT) d = mfma(kop, q[r].lo[y], d);
+                            d = mfma(kop, q[r].hi[y], d);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) sc[r][4 * h + j] = fmaf(kd.at(y, 4 * h + j), d[j], y == 0 ? 0.f : sc[r][4 * h + j]);
                         }

@@ -45,8 +45,8 @@ constexpr int kMinPart = 4;
 constexpr int kRowTiles = 1;
 
 // Workgroups of four waves that a CU holds, by the registers of a wave: its
-// sums, queries with where their dots start (16-bit rows) or their second
-// parts (fp32), a tile of codes and scales, and what the work on them takes (found by compiling): three within 168, two
+// sums, queries (with the second parts of fp32 rows), a tile of codes and
+// scales, and what the work on them takes (found by compiling): three within 168, two
 // within 256, else one.
 QBD_HD constexpr int split_groups_a_cu(int kbits, int vbits, int nb, int rt) {
     const int kept = 16 * nb * rt + nb * (kbits / 2 + vbits / 2 + 8) + 90 + 25 * (rt - 1);

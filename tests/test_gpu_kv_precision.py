@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import block_quantized_decode_amd as qbd
-from kv_util import Cache, check_attention, device, gpu, kv, note
+from kv_util import DTYPES, Cache, check_attention, device, gpu, kv, note
 from test_gpu_kv import FORMATS, layout
 
 pytestmark = pytest.mark.gpu
@@ -35,3 +35,30 @@ def test_fp32_scores_of_keys_with_an_outlier_that_the_query_compensates(new, dim
     for hints in ({}, dict(max_q=new, max_len=60)):
         out = qbd.kv_attention(gpu(q), *cache.planes, gpu(table), gpu(np.array(lens, dtype=np.int32)), q_starts=gpu(starts), scale=1.0, **hints)
         check_attention("compensated outliers", out, ref, mass, reach, 60, "f32")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("vbits", [4, 8])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 9])
+def test_16_bit_scores_of_keys_with_an_outlier_that_the_query_compensates(new, dim, vbits, dtype):
+    """The same with rows of 16 bits, whose factors keep 11, and a mean further above the outlier's channel."""
+    rng = np.random.default_rng(dim + new)
+    lens, page, heads, group = [5, 41, 60], 16, 2, 3
+    table, pages = layout(rng, page, lens)
+    cache = Cache(rng, pages, heads, page, dim, 8, vbits)
+    nb = dim // 32
+    at = np.arange(nb) * 32 + rng.integers(0, 32, size=nb)
+    cache.codes[0][:] = 0
+    cache.codes[0][..., at] = rng.choice([-127, 127], size=(pages, heads, page, nb))
+    cache.scales[0][:] = rng.uniform(0.2, 0.3, size=cache.scales[0].shape)
+    cache.upload()
+    q = 400 + 200 * rng.standard_normal((3 * new, heads * group, dim))
+    q[..., at] = rng.standard_normal((3 * new, heads * group, nb)) * 0.5 / 127
+    q = torch.from_numpy(q.astype(np.float32)).to(device()).to(DTYPES[dtype])
+    starts = (np.arange(4) * new).astype(np.int32)
+    note("kv attention compensated outliers", new, dim, vbits, dtype)
+    ref, mass, reach = kv.attention(q.double().cpu().numpy(), cache.k, cache.v, table, lens, starts, scale=1.0)
+    for hints in ({}, dict(max_q=new, max_len=60)):
+        out = qbd.kv_attention(q, *cache.planes, gpu(table), gpu(np.array(lens, dtype=np.int32)), q_starts=gpu(starts), scale=1.0, **hints)
+        check_attention("compensated outliers", out, ref, mass, reach, 60, dtype, np.abs(cache.v).max())
