@@ -21,6 +21,11 @@ constexpr float kNoKey = -3e38f;  // reference of a row that has seen no key
 // weights far below the largest keep their bits (11 down to 2^-28 of it).
 constexpr float kLift = 12.f, kTop = 15.f;
 
+// A query row enters scaled by a power of two to a maximum of 2^14 or more,
+// below 2^15, so that its elements keep a binary16 number's 11 bits down to
+// 2^-28 of the largest.
+constexpr int kQueryTop = 15;
+
 __device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 
 __device__ __forceinline__ f4 mfma(u4 a, u4 b, f4 c) {  // eight bf16 each

@@ -83,8 +83,8 @@ __device__ __forceinline__ u4 lds_read(uint32_t place) {
 }
 
 // A row in operand order for steps of 16 elements (chunk 2x + half of K's
-// order is 4b + g), scaled to a maximum near 1; returns the factor of its
-// scores in units of log2.
+// order is 4b + g), scaled (kQueryTop); returns the factor of its scores in
+// units of log2.
 template <int KB, int NB>
 __device__ __forceinline__ float load_query(const AttnArgs& a, int64_t at, int half, h8 (&q)[2 * NB]) {
     constexpr int kRun = KB == 4 ? 16 : 4;
@@ -102,7 +102,7 @@ __device__ __forceinline__ float load_query(const AttnArgs& a, int64_t at, int h
         for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(raw[x][i / 4].at(i % 4, a.elem)));
     }
     top = fmaxf(top, __shfl_xor(top, 32));
-    const int e = __builtin_amdgcn_frexp_expf(top);
+    const int e = __builtin_amdgcn_frexp_expf(top) - kQueryTop;
     const float sign = a.scale < 0.f ? -1.f : 1.f;
 #pragma unroll
     for (int x = 0; x < 2 * NB; ++x) {

@@ -21,13 +21,13 @@
 // second product: the weights never leave their lane.  The cache stores V
 // by eight keys so that this operand is one load as well.
 //
-// Roundings: q is scaled by a power of two to a row maximum near 1 and
-// rounded to binary16, exact for bf16 and f16 rows up to 2^-25 of that
-// maximum; f32 rows add a second binary16 for the remainder (22 bits).  A
-// weight times its V scale is rounded to binary16 (11 bits, below the
-// output's rounding); for f32 outputs it enters exactly, as three bf16 parts
-// of 8 bits, so that a sum keeps its precision however far its weights lie
-// below the largest.
+// Roundings: q is scaled by a power of two (kQueryTop) and rounded to
+// binary16, exact for bf16 and f16 elements down to 2^-28 of the row's
+// largest; f32 rows add a second binary16 for the remainder (22 bits, down to
+// 2^-17).  A weight times its V scale is rounded to binary16 (11 bits: as
+// coarse as an f16 output, whose error is a third above one rounding alone);
+// for f32 outputs it enters exactly, as three bf16 parts of 8 bits, so that a
+// sum keeps its precision however far its weights lie below the largest.
 // With binary16 the reference R of a row counts the largest V scale in, so
 // that these products use the type's range whatever the size of the values.
 // R only moves when a tile passes it by 2^(kTop - kLift), so most tiles
@@ -220,8 +220,8 @@ __device__ __forceinline__ int find_sequence(const AttnArgs& a, const Split& sp,
 
 
 
-// A lane's part of a query row in operand order, scaled by a power of two to
-// a maximum near 2^10.  The codes that it meets are the exact ones: entered with
+// A lane's part of a query row in operand order, scaled (kQueryTop).  The
+// codes that it meets are the exact ones: entered with
 // an offset (fewer instructions) they make a block's dot the difference of two
 // larger sums, whose fp32 roundings were up to some hundred times the dot's own
 // where a block's codes are small (an outlier beside them, queries with a mean).
@@ -249,7 +249,7 @@ struct Query {
         }
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        const int e = __builtin_amdgcn_frexp_expf(top) - 10;
+        const int e = __builtin_amdgcn_frexp_expf(top) - kQueryTop;
         const float sign = a.scale < 0.f ? -1.f : 1.f;
         c = ldexpf(fabsf(a.scale) * 1.44269504088896340736f, e);
 #pragma unroll

@@ -282,9 +282,11 @@ int kv_cache_read(const qbd_kv_cache* cache, const int64_t* slots, int64_t T, in
  * order.
  * q is laid out as k above; out is [T][qheads][dim], contiguous, in dtype.
  * Scores, softmax statistics and sums are fp32.  With dtype F32 a factor of
- * a score carries at least 22 significant bits and the weights enter in
- * full; with BF16 and F16 (and for prompts, K and V) they carry 11, and a
- * weight below 2^-28 of its row's largest fewer (below 2^-37 none).
+ * a score carries at least 22 significant bits (an element of q below 2^-17
+ * of its row's largest fewer) and the weights enter in full; with BF16 and
+ * F16 the elements of q and the weights (and for prompts, those of K and V)
+ * carry 11, and an element of q or a weight below 2^-28 of its row's largest
+ * fewer (a weight below 2^-37 none).
  * work is a scratch buffer of kv_attention_work_bytes(...) bytes, 256-byte
  * aligned; its contents need no preparation and mean nothing afterwards.
  */

@@ -62,3 +62,41 @@ def test_16_bit_scores_of_keys_with_an_outlier_that_the_query_compensates(new, d
     for hints in ({}, dict(max_q=new, max_len=60)):
         out = qbd.kv_attention(q, *cache.planes, gpu(table), gpu(np.array(lens, dtype=np.int32)), q_starts=gpu(starts), scale=1.0, **hints)
         check_attention("compensated outliers", out, ref, mass, reach, 60, dtype, np.abs(cache.v).max())
+
+
+HEADS, GROUP = 8, 2
+
+
+def prompt(cache, table, lens, news, q, window=0):
+    """Rows enough for the prompt kernel, where news are."""
+    starts = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+    return qbd.kv_attention(q, *cache.planes, gpu(table), gpu(np.array(lens, dtype=np.int32)), q_starts=gpu(starts), max_q=max(news),
+                            max_len=32768, window=window, scale=1.0), starts
+
+
+def queries(rng, tokens, dim, dtype, spread):
+    q = torch.from_numpy((rng.standard_normal((tokens, HEADS * GROUP, dim)) * spread).astype(np.float32)).to(device()).to(dtype)
+    return q, q.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("news", [[1, 1], [9, 5], [300, 280]])
+@pytest.mark.parametrize("dim,kbits", [(64, 4), (128, 8), (256, 4)])
+def test_small_elements_of_a_query_keep_their_bits(dim, kbits, news, dtype):
+    """A channel whose queries are a millionth of their row's others, and whose keys are as much larger."""
+    rng = np.random.default_rng(dim + 2)
+    lens, page = [330, 290], 32
+    table, pages = layout(rng, page, lens)
+    cache = Cache(rng, pages, HEADS, page, dim, kbits, 4, kscale=(1e-5, 3e-5))
+    codes, scales = cache.codes[0].reshape(pages, HEADS, page, dim // 32, 32), cache.scales[0]
+    large = rng.random(scales.shape) < 0.1
+    codes[large] = 0
+    codes[large, 5], codes[large, 21] = 1, -1
+    scales[large] = rng.uniform(100, 250, size=int(large.sum()))
+    cache.upload()
+    q, _ = queries(rng, sum(news), dim, DTYPES[dtype], 3000.0)
+    q.view(*q.shape[:2], -1, 32)[..., [5, 21]] *= 1e-6
+    note("kv small elements of a query", dim, kbits, news, dtype)
+    out, starts = prompt(cache, table, lens, news, q)
+    ref, mass, reach = kv.attention(q.double().cpu().numpy(), cache.k, cache.v, table, lens, starts, scale=1.0)
+    check_attention("small elements", out, ref, mass, reach, max(lens), dtype, np.abs(cache.v).max())
