@@ -35,8 +35,12 @@
 // Roundings (11 bits each): an element d * code, exact in 18 bits, a weight
 // relative to its row's running maximum; q is scaled by a power of two as in
 // the split kernel.  d * code is a multiple of the type's smallest step, so
-// it is exact or good to 11 bits however small; a tile with a scale above
-// 256 enters with its scales times 2^-8, so it does not overflow either.
+// it is exact or good to 11 bits however small.  It overflows where d is above
+// 256: such a block enters times 2^-8, block by block, and in a tile that has
+// one the products over those blocks are made once more and 255 times their
+// result is added (1024 rows of 32 over 8 heads, 8192 keys of 128: 1.6 times as
+// long with such a K block in every tile, 1.4 with one of V, 2.1 and 1.8 where
+// all are).  What keys that no row sees hold can cost that, but changes no bit.
 #pragma once
 
 #include "kv_attn.hpp"
@@ -265,20 +269,19 @@ __global__ __launch_bounds__(64 * W, kv_plan::prompt_groups_a_cu(NB, W) * W / 4)
         }
         if (lane == 0) notes[n & 3] = flags;
     };
-    // The fetched scales made fit, before their tile is expanded.
-    int flags_next = 0, big_v = 0;  // once a V scale is large, all that follow are reduced
+    // The fetched scales made fit, before their tile is expanded: those above
+    // 256 times 2^-8, none for a V key that is not there or is no number.
+    int flags_next = 0;
+    auto large = [](uint32_t d) { return (d & 0x7fffu) > 0x5c00u; };  // a NaN too
     auto adjust = [&](int j) {
-        const int flags = uniform(notes[(j - first) & 3]);
-        big_v |= flags & 2;
-        const bool nan_v = flags & 4;
-        flags_next = flags | big_v;
-        if (flags & 1) {
+        flags_next = uniform(notes[(j - first) & 3]);
+        if (flags_next & 1) {
 #pragma unroll
-            for (int y = 0; y < NBT; ++y) f.kd[y] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(as_h2(f.kd[y])[0] * 0.00390625f16));
+            for (int y = 0; y < NBT; ++y) f.kd[y] = large(f.kd[y]) ? __builtin_bit_cast(uint16_t, static_cast<_Float16>(as_h2(f.kd[y])[0] * 0.00390625f16)) : f.kd[y];
         }
         const int t = begin + j * BN + 16 * unit;
         const bool ok = held_next >> unit & 1;
-        if (!ok || t + 16 > end || nan_v) {  // no scale for a key that is not there or whose scale is no number
+        if (!ok || t + 16 > end || (flags_next & 4)) {
 #pragma unroll
             for (int i = 0; i < 4 * Z; ++i) {
                 const int key = t + 8 * vz + 2 * i;
@@ -288,9 +291,13 @@ __global__ __launch_bounds__(64 * W, kv_plan::prompt_groups_a_cu(NB, W) * W / 4)
                 w &= (x ? 0xffffu : 0u) | (y ? 0xffff0000u : 0u);
             }
         }
-        if (big_v) {
+        if (flags_next & 2) {
 #pragma unroll
-            for (int i = 0; i < 4 * Z; ++i) f.vd[i / 4][i % 4] = __builtin_bit_cast(uint32_t, as_h2(f.vd[i / 4][i % 4]) * h2{0.00390625f16, 0.00390625f16});
+            for (int i = 0; i < 4 * Z; ++i) {
+                uint32_t& w = f.vd[i / 4][i % 4];
+                const uint32_t less = __builtin_bit_cast(uint32_t, as_h2(w) * h2{0.00390625f16, 0.00390625f16});
+                w = ((large(w) ? less : w) & 0xffffu) | ((large(w >> 16) ? less : w) & 0xffff0000u);
+            }
         }
         held = held_next;
     };
@@ -331,7 +338,7 @@ __global__ __launch_bounds__(64 * W, kv_plan::prompt_groups_a_cu(NB, W) * W / 4)
         for (int i = 0; i < kPieces; ++i) expand(o, i);
     };
 
-    int held_lds = 0, reduced = 0;
+    int held_lds = 0;
     const int count = stop - first;
     if (count > 0) {
         find(0);
@@ -388,6 +395,16 @@ __global__ __launch_bounds__(64 * W, kv_plan::prompt_groups_a_cu(NB, W) * W / 4)
             const uint32_t place = at_v ^ (32 * (BN == 64 ? y ^ (x & 3) : y));
             return __builtin_bit_cast(h8, lds_read(place + 32 * x * 2 * BN));
         };
+        // (a tile with notes) which of its keys have a scale in block x that
+        // asks(d) is about: a key a lane
+        auto keys_where = [&](const uint16_t* scales, int x, auto asks) {
+            const int u = min(lane / 16, UNITS - 1), t = t0 + 16 * u + lane % 16;
+            const int64_t page = t < end ? table[t >> shift] : -1;
+            const bool ok = lane < BN && page >= 0 && page < a.kv.pages;
+            const int64_t at = (((ok ? page : 0) * a.kv.heads + head) << shift) + (t & mask);
+            const uint32_t d = ok ? scales[(at & ~int64_t{7}) * NB + 8 * x + (at & 7)] : 0;
+            return __ballot(asks(d));
+        };
         // scores of step n, work(x) between the products
         auto score = [&](int n, auto work) {
             h8 next[2] = {k_operand(n, 0), k_operand(n, 1)};
@@ -406,7 +423,21 @@ __global__ __launch_bounds__(64 * W, kv_plan::prompt_groups_a_cu(NB, W) * W / 4)
         // masks, and a reference that the step's scores fit; the weights of
         // `made` steps before it in this tile move with it
         auto settle = [&](int n, int made) {
-            if (flags & 1) sc[n] *= 256.f;
+            if (flags & 1) {  // blocks of K that entered times 2^-8
+#pragma unroll
+                for (int x = 0; x < NB; ++x) {
+                    const uint32_t keys = static_cast<uint32_t>(keys_where(a.kv.kd, x, large) >> (32 * n));
+                    if (keys == 0) continue;
+                    f16v part;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) part[i] = 0.f;
+                    part = mfma32(k_operand(n, 2 * x), q[2 * x], part);
+                    part = mfma32(k_operand(n, 2 * x + 1), q[2 * x + 1], part);
+                    const uint32_t mine = keys >> (4 * half);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sc[n][i] = mine >> (8 * (i / 4) + i % 4) & 1 ? fmaf(255.f, part[i], sc[n][i]) : sc[n][i];
+                }
+            }
             if (masked) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -474,11 +505,6 @@ __global__ __launch_bounds__(64 * W, kv_plan::prompt_groups_a_cu(NB, W) * W / 4)
             for (int i = x * kPieces / (2 * NB); i < (x + 1) * kPieces / (2 * NB); ++i) expand(out, i);
         });
         ahead(n);
-        if ((flags & 2) && !reduced) {  // V enters times 2^-8 from here on
-            reduced = 1;
-#pragma unroll
-            for (int x = 0; x < NB; ++x) acc[x] *= 0.00390625f;
-        }
         settle(0, 0);
         if constexpr (STEPS == 2) {
             score(1, [&](int x) { weigh_piece(0, x); });
@@ -490,15 +516,30 @@ __global__ __launch_bounds__(64 * W, kv_plan::prompt_groups_a_cu(NB, W) * W / 4)
             for (int x = 0; x < 2 * NB; ++x) weigh_piece(0, x);
             add(0, nothing);
         }
-        if (flags & 4) {  // a V scale that is no number spoils the rows that see it
-            const int u = min(lane / 16, UNITS - 1), t = t0 + 16 * u + lane % 16;
-            const int64_t page = t < end ? table[t >> shift] : -1;
-            const bool ok = lane < BN && page >= 0 && page < a.kv.pages;
-            const int64_t at = (((ok ? page : 0) * a.kv.heads + head) << shift) + (t & mask);
+        if (flags & 2) {  // blocks of V that entered times 2^-8
 #pragma unroll
             for (int x = 0; x < NB; ++x) {
-                const uint16_t d = ok ? a.kv.vd[(at & ~int64_t{7}) * NB + 8 * x + (at & 7)] : 0;
-                const uint64_t bad = __ballot((d & 0x7c00) == 0x7c00);
+                const uint64_t keys = keys_where(a.kv.vd, x, [&](uint32_t d) { return large(d) && (d & 0x7c00) != 0x7c00; });
+                if (keys == 0) continue;
+                f16v part;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) part[i] = 0.f;
+#pragma unroll
+                for (int u = 0; u < UNITS; ++u) {
+                    const uint32_t mine = static_cast<uint32_t>(keys >> (16 * u)) >> (4 * half);
+                    h8 w = p[u];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i] = mine >> (8 * (i / 4) + i / 2 % 2 + 2 * (i % 2)) & 1 ? w[i] : 0.f16;
+                    part = mfma32(v_operand(u * NB + x), w, part);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[x][i] = fmaf(255.f, part[i], acc[x][i]);
+            }
+        }
+        if (flags & 4) {  // a V scale that is no number spoils the rows that see it
+#pragma unroll
+            for (int x = 0; x < NB; ++x) {
+                const uint64_t bad = keys_where(a.kv.vd, x, [](uint32_t d) { return (d & 0x7c00) == 0x7c00; });
                 const int lo = min(max(lo_r - t0, 0), BN), hi = min(max(min(hi_r, s.len) - t0, 0), BN);
                 const uint64_t below = hi >= 64 ? ~uint64_t{0} : (uint64_t{1} << hi) - 1;
                 const uint64_t seen = lo >= 64 ? 0 : below & ~((uint64_t{1} << lo) - 1);
@@ -510,10 +551,6 @@ __global__ __launch_bounds__(64 * W, kv_plan::prompt_groups_a_cu(NB, W) * W / 4)
         }
     }
 
-    if (reduced) {
-#pragma unroll
-        for (int x = 0; x < NB; ++x) acc[x] *= 256.f;
-    }
     sum += __shfl_xor(sum, 32);
     const int at_row = 32 * wave + (lane & 31);
     if (at_row < rows && parts > 1) {

@@ -100,3 +100,93 @@ def test_small_elements_of_a_query_keep_their_bits(dim, kbits, news, dtype):
     out, starts = prompt(cache, table, lens, news, q)
     ref, mass, reach = kv.attention(q.double().cpu().numpy(), cache.k, cache.v, table, lens, starts, scale=1.0)
     check_attention("small elements", out, ref, mass, reach, max(lens), dtype, np.abs(cache.v).max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim,kbits,vbits", [(64, 4, 4), (96, 8, 4), (128, 4, 4), (128, 8, 8), (192, 8, 4), (256, 8, 8)])
+def test_prompts_keep_small_values_beside_large_scales(dim, kbits, vbits, dtype):
+    """V blocks with a scale above 256 here and there, some with small codes in them, among values of a thousandth."""
+    rng = np.random.default_rng(dim)
+    lens, news, page = [330, 290], [300, 280], 32
+    table, pages = layout(rng, page, lens)
+    cache = Cache(rng, pages, HEADS, page, dim, kbits, vbits, kscale=(0.002, 0.01), vscale=(2e-4, 2e-3))
+    codes, scales = cache.codes[1].reshape(pages, HEADS, page, dim // 32, 32), cache.scales[1]
+    large = rng.random(scales.shape) < 0.03
+    scales[large] = rng.uniform(300, 60000, size=int(large.sum()))
+    codes[large] = 0
+    cache.upload()
+    q, q64 = queries(rng, sum(news), dim, DTYPES[dtype], 1.0)
+    note("kv prompts small beside large", dim, kbits, vbits, dtype)
+    out, starts = prompt(cache, table, lens, news, q)
+    ref, mass, reach = kv.attention(q64, cache.k, cache.v, table, lens, starts, scale=1.0)
+    check_attention("V", out, ref, mass, reach, max(lens), dtype, np.abs(cache.v).max())
+    # and the large blocks themselves, where the output's type holds them
+    codes[large] = np.where(rng.random(codes[large].shape) < 0.1, 1, 0)
+    scales[large] = rng.uniform(300, 1000, size=int(large.sum()))
+    cache.upload()
+    out, starts = prompt(cache, table, lens, news, q)
+    ref, mass, reach = kv.attention(q64, cache.k, cache.v, table, lens, starts, scale=1.0)
+    check_attention("large V", out, ref, mass, reach, max(lens), dtype, np.abs(cache.v).max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim,kbits,vbits", [(64, 4, 4), (96, 8, 4), (128, 4, 4), (128, 8, 8), (192, 8, 4), (256, 8, 8)])
+def test_prompts_keep_small_keys_beside_large_scales(dim, kbits, vbits, dtype):
+    """K blocks with a scale above 256 here and there, of zeros or of one small code, among scales of 1e-5 that queries in
+    the thousands make up for."""
+    rng = np.random.default_rng(dim + 1)
+    lens, news, page = [330, 290], [300, 280], 32
+    table, pages = layout(rng, page, lens)
+    cache = Cache(rng, pages, HEADS, page, dim, kbits, vbits, kscale=(1e-5, 3e-5))
+    codes, scales = cache.codes[0].reshape(pages, HEADS, page, dim // 32, 32), cache.scales[0]
+    large = rng.random(scales.shape) < 0.03
+    scales[large] = rng.uniform(300, 60000, size=int(large.sum()))
+    codes[large] = 0
+    cache.upload()
+    q, q64 = queries(rng, sum(news), dim, DTYPES[dtype], 3000.0)
+    note("kv prompts small keys beside large", dim, kbits, vbits, dtype)
+    out, starts = prompt(cache, table, lens, news, q)
+    ref, mass, reach = kv.attention(q64, cache.k, cache.v, table, lens, starts, scale=1.0)
+    check_attention("K", out, ref, mass, reach, max(lens), dtype, np.abs(cache.v).max())
+    # the large blocks take part: one code, in a channel whose queries are small
+    codes[large, 5] = 1
+    scales[large] = rng.uniform(300, 1000, size=int(large.sum()))
+    q.view(*q.shape[:2], -1, 32)[..., 5] *= 1e-6
+    cache.upload()
+    out, starts = prompt(cache, table, lens, news, q)
+    ref, mass, reach = kv.attention(q.double().cpu().numpy(), cache.k, cache.v, table, lens, starts, scale=1.0)
+    check_attention("large K", out, ref, mass, reach, max(lens), dtype, np.abs(cache.v).max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("window", [0, 37])
+@pytest.mark.parametrize("news", [[300, 280, 260]])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_hidden_bytes_change_no_bit(dim, news, window, dtype):
+    """NaN, infinite, large and ordinary scales in every place that no row sees: past a sequence's end, before its first
+    row's window, in pages that it does not hold and where page 0 stands for those; the visible scales are small."""
+    rng = np.random.default_rng(dim + window)
+    lens, page = [330, 301, 275], 32
+    table, pages = layout(rng, page, lens)
+    pages += 1
+    table = np.where(table >= 0, table + 1, table)  # page 0 is nobody's
+    table[0, [2, 10]], table[1, 8] = -1, pages + 5
+    cache = Cache(rng, pages, HEADS, page, dim, 8, 4, kscale=(1e-4, 1e-3), vscale=(1e-4, 1e-3))
+    hidden = np.ones((pages, page), bool)
+    for b, (n, new) in enumerate(zip(lens, news)):
+        first = max(0, n - new + 1 - window) if window else 0
+        for t in range(first, n):
+            if 0 <= table[b, t // page] < pages:
+                hidden[table[b, t // page], t % page] = False
+    q, q64 = queries(rng, sum(news), dim, DTYPES[dtype], 30.0)
+    note("kv hidden bytes", dim, news, window, dtype)
+    clean, starts = prompt(cache, table, lens, news, q, window)
+    ref, mass, reach = kv.attention(q64, cache.k, cache.v, table, lens, starts, window=window, scale=1.0)
+    check_attention("clean", clean, ref, mass, reach, max(lens), dtype, np.abs(cache.v).max())
+    for fill in ([300.0, 40000.0], [np.nan, np.inf, -np.inf], [0.5, 3.0, 1e-7], [np.nan, 500.0, 2e-4, 0.0]):
+        for codes, scales in zip(cache.codes, cache.scales):
+            at = np.broadcast_to(hidden[:, None], scales.shape[:3])
+            scales[at] = rng.choice(fill, size=(int(at.sum()), scales.shape[3])).astype(np.float16)
+            codes[at] = rng.integers(-7, 8, size=(int(at.sum()), dim))
+        cache.upload()
+        assert torch.equal(prompt(cache, table, lens, news, q, window)[0], clean), fill
