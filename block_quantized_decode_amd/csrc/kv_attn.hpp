@@ -46,18 +46,17 @@ __device__ __forceinline__ uint32_t cut8(float& a, float& b) {
 __device__ __forceinline__ h2 as_h2(uint32_t w) { return __builtin_bit_cast(h2, w); }
 __device__ __forceinline__ h8 as_h8(h2 a, h2 b, h2 c, h2 d) { return h8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]}; }
 
-// The binary16 pair (1024, 1024) in a vector register, so that the and-or
-// below is one instruction (it takes a single scalar operand).
+// The binary16 pair (1024, 1024) in a vector register, of a value that the
+// compiler does not know, so that the and-or below is one instruction (it takes
+// a single scalar operand).  No asm statement here holds an instruction: the
+// compiler counts the states that the matrix instructions have to wait for
+// between its own instructions alone.
 __device__ __forceinline__ uint32_t pair1024() {
-    uint32_t v;
-    asm("v_mov_b32 %0, 0x64006400" : "=v"(v));
+    uint32_t v = 0x64006400u;
+    asm("" : "+v"(v));
     return v;
 }
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t high) {
-    uint32_t r;
-    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(w), "s"(mask), "v"(high));
-    return r;
-}
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t high) { return (w & mask) | high; }
 
 // Nibbles 0 and 4 (low) or 1 and 5 (high) of w as exact q - 8: 0x6400 | n
 // is 1024 + n in binary16, and with the nibble four places up 1024 + 16 n.

@@ -264,18 +264,12 @@ struct Query {
     }
 };
 
-// p0 d.lo and p1 d.hi (DLO, DHI: halves of d0, d1), rounded once to binary16
-// each; p in fp32, d in binary16.
-template <int H0, int H1>
+// p0 times half H of d0 and p1 times half H of d1, rounded to binary16 (the
+// sum with zero lets the compiler take one mixed-precision instruction each).
+template <int H>
 __device__ __forceinline__ h2 weigh_pair(float p0, float p1, uint32_t d0, uint32_t d1) {
-    uint32_t r;
-    if constexpr (H0 == 0 && H1 == 0)
-        asm("v_fma_mixlo_f16 %0, %1, %3, 0 op_sel_hi:[0,1,0]\n\tv_fma_mixhi_f16 %0, %2, %4, 0 op_sel_hi:[0,1,0]"
-            : "=&v"(r) : "v"(p0), "v"(p1), "v"(d0), "v"(d1));
-    else
-        asm("v_fma_mixlo_f16 %0, %1, %3, 0 op_sel:[0,1,0] op_sel_hi:[0,1,0]\n\tv_fma_mixhi_f16 %0, %2, %4, 0 op_sel:[0,1,0] op_sel_hi:[0,1,0]"
-            : "=&v"(r) : "v"(p0), "v"(p1), "v"(d0), "v"(d1));
-    return as_h2(r);
+    return h2{static_cast<_Float16>(__builtin_fmaf(p0, static_cast<float>(as_h2(d0)[H]), 0.f)),
+              static_cast<_Float16>(__builtin_fmaf(p1, static_cast<float>(as_h2(d1)[H]), 0.f))};
 }
 
 template <int KB, int VB, int NB, int RT, bool SPLIT>
@@ -546,8 +540,8 @@ __global__ __launch_bounds__(256, kv_plan::split_groups_a_cu(KB, VB, NB, RT)) vo
                         for (int r = 0; r < RT; ++r) {
                             const uint32_t* dv = vd.w + 4 * y;
                             const float* p = sc[r];
-                            h8 x = as_h8(weigh_pair<0, 0>(p[0], p[2], dv[0], dv[1]), weigh_pair<1, 1>(p[1], p[3], dv[0], dv[1]),
-                                         weigh_pair<0, 0>(p[4], p[6], dv[2], dv[3]), weigh_pair<1, 1>(p[5], p[7], dv[2], dv[3]));
+                            h8 x = as_h8(weigh_pair<0>(p[0], p[2], dv[0], dv[1]), weigh_pair<1>(p[1], p[3], dv[0], dv[1]),
+                                         weigh_pair<0>(p[4], p[6], dv[2], dv[3]), weigh_pair<1>(p[5], p[7], dv[2], dv[3]));
                             if (masked) {  // a NaN scale of a key that another row sees
                                 constexpr int order[8] = {0, 2, 1, 3, 4, 6, 5, 7};
 #pragma unroll
