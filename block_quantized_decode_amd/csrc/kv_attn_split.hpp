@@ -463,11 +463,14 @@ __global__ __launch_bounds__(256, kv_plan::split_groups_a_cu(KB, VB, NB, RT)) vo
                             sc[r][j] = see ? sc[r][j] : -INFINITY;
                         }
                     }
-                    if constexpr (!SPLIT) {  // scales of keys that no row sees may hold anything
+                    if constexpr (!SPLIT) {  // scales of keys that the lane's rows do not see may hold anything
+                        uint32_t any = 0;
+#pragma unroll
+                        for (int r = 0; r < RT; ++r) any |= seen[r];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            uint32_t keep = mine && tg + 2 * j < s.len ? 0xffffu : 0u;
-                            keep |= mine && tg + 2 * j + 1 < s.len ? 0xffff0000u : 0u;
+                            uint32_t keep = any >> (2 * j) & 1 ? 0xffffu : 0u;
+                            keep |= any >> (2 * j + 1) & 1 ? 0xffff0000u : 0u;
 #pragma unroll
                             for (int y = 0; y < NB; ++y) vd.w[4 * y + j] &= keep;
                         }
@@ -542,7 +545,7 @@ __global__ __launch_bounds__(256, kv_plan::split_groups_a_cu(KB, VB, NB, RT)) vo
                             const float* p = sc[r];
                             h8 x = as_h8(weigh_pair<0>(p[0], p[2], dv[0], dv[1]), weigh_pair<1>(p[1], p[3], dv[0], dv[1]),
                                          weigh_pair<0>(p[4], p[6], dv[2], dv[3]), weigh_pair<1>(p[5], p[7], dv[2], dv[3]));
-                            if (masked) {  // a NaN scale of a key that another row sees
+                            if (RT > 1 && masked) {  // a NaN scale of a key that another of the lane's rows sees
                                 constexpr int order[8] = {0, 2, 1, 3, 4, 6, 5, 7};
 #pragma unroll
                                 for (int j = 0; j < 8; ++j) x[j] = seen[r] >> order[j] & 1 ? x[j] : 0.f16;

@@ -160,7 +160,7 @@ def test_prompts_keep_small_keys_beside_large_scales(dim, kbits, vbits, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("window", [0, 37])
-@pytest.mark.parametrize("news", [[300, 280, 260]])
+@pytest.mark.parametrize("news", [[1, 1, 1], [9, 5, 7], [300, 280, 260]])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_hidden_bytes_change_no_bit(dim, news, window, dtype):
     """NaN, infinite, large and ordinary scales in every place that no row sees: past a sequence's end, before its first
