@@ -132,6 +132,8 @@ QBD_HD constexpr int prompt_groups_a_cu(int nb, int waves) {
 // host does not know counts as 16384 keys; a window as its keys and the rows',
 // but never as more than the length would without it, so that the workspace,
 // whose size is asked without the window, holds whatever it chooses.
+// The sequences' rows together are no more than the tokens', and without a
+// bound on a sequence's their average has to be a prompt's.
 constexpr int kPromptRows = 96;
 constexpr double kPromptWork = 40e6;
 constexpr int64_t kPromptKeys = 32768;  // longer counts as this
@@ -142,7 +144,9 @@ constexpr PromptPlan prompt_plan(int dim, int heads, int qheads, int64_t batch, 
     const int64_t rows = most_rows(qheads / heads, T, max_q);
     const int64_t known = most_keys(T, max_q, max_len, window), most_counted = max_len > 0 ? kPromptKeys : kPromptKeys / 2;
     const int64_t keys = known == 0 || known > most_counted ? most_counted : known;
-    if (rows < kPromptRows || static_cast<double>(rows) * heads * batch * (keys + 1300) < kPromptWork) return PromptPlan{0, 0, 1};
+    const double all = static_cast<double>(qheads / heads) * T, each = static_cast<double>(rows) * batch;
+    if (rows < kPromptRows || (max_q == 0 && all < static_cast<double>(kPromptRows) * batch)) return PromptPlan{0, 0, 1};
+    if ((each < all ? each : all) * heads * (keys + 1300) < kPromptWork) return PromptPlan{0, 0, 1};
     const int take = (dim == 64 || dim == 128) && rows > 128 ? 256 : 128;
     const int64_t tiles = (rows + take - 1) / take, fill = 256 * prompt_groups_a_cu(dim / 32, take / 32);
     const double groups = static_cast<double>(tiles) * heads * batch;

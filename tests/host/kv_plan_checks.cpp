@@ -136,6 +136,39 @@ void check_row_count() {
         }
 }
 
+// Without a bound on a sequence's rows the tokens of all are shared among
+// them: a batch of single tokens is not taken for prompts, prompts still are.
+void check_unknown_rows() {
+    using namespace qbd::kv_plan;
+    auto rows = [](const Shape& s) {
+        int64_t need = 0;
+        if (attend(s, need) != QBD_OK) ++g_failures;
+        return prompt_plan(g_attn.kv.dim, g_attn.kv.heads, g_attn.qheads, g_attn.batch, g_attn.T, g_attn.max_q, g_attn.max_len, g_attn.window).rows;
+    };
+    for (int64_t dim : {64, 128, 256})
+        for (int64_t heads : {1, 8})
+            for (int64_t group : {1, 4, 7})
+                for (int64_t max_len : {0, 500, 8192, 100000}) {
+                    for (int64_t batch : {1, 32, 64, 256, 4096})
+                        for (int64_t each : {1, 8}) {
+                            const Shape s = {dim, heads, group, batch, batch * each, 0, max_len, 0};
+                            if (each * group < kPromptRows && rows(s) != 0) {
+                                std::fprintf(stderr, "%lld x %lld tokens of %lld over %lld heads, max_len %lld: taken for prompts\n", (long long)batch,
+                                             (long long)each, (long long)(heads * group), (long long)heads, (long long)max_len);
+                                ++g_failures;
+                            }
+                        }
+                    // the same answer as with the bound, where the sequences are alike
+                    for (int64_t batch : {1, 4, 16})
+                        for (int64_t each : {100, 600, 2000})
+                            if ((rows({dim, heads, group, batch, batch * each, 0, max_len, 0}) > 0) !=
+                                (rows({dim, heads, group, batch, batch * each, each, max_len, 0}) > 0)) {
+                                std::fprintf(stderr, "%lld x %lld tokens: not what the bound gives\n", (long long)batch, (long long)each);
+                                ++g_failures;
+                            }
+                }
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
@@ -143,6 +176,7 @@ int main(int argc, char** argv) {
     if (!std::strcmp(which, "window_workspace")) check_window_workspace();
     else if (!std::strcmp(which, "window_range")) check_window_range();
     else if (!std::strcmp(which, "row_count")) check_row_count();
+    else if (!std::strcmp(which, "unknown_rows")) check_unknown_rows();
     else return 2;
     if (g_failures) return 1;
     std::printf("%s passed\n", which);

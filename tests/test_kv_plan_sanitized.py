@@ -40,3 +40,7 @@ def test_windows_near_the_types_limit_reach_the_kernels_in_range(checks):
 
 def test_rows_of_a_head_are_refused_where_32_bits_do_not_count_them(checks):
     checks("row_count")
+
+
+def test_batches_of_single_tokens_are_not_taken_for_prompts(checks):
+    checks("unknown_rows")
