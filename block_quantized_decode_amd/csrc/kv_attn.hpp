@@ -15,6 +15,10 @@ typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
 constexpr float kNoKey = -3e38f;  // reference of a row that has seen no key
+// Beyond this a reference and the scores near it are rounded by more than a
+// fused multiply-add's own rounding may differ from them: once a row's reference
+// is there, its wave finds the weights' exponents from rounded products.
+constexpr float kLargeRef = 1048576.f;
 // A product of a weight and a V scale enters the matrix cores in binary16.
 // The reference puts the largest at 2^kLift, and it may grow to 2^kTop
 // before the reference moves: near the top of the type's range, so that

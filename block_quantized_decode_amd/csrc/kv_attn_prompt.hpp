@@ -184,6 +184,7 @@ __global__ __launch_bounds__(64 * W, kv_plan::prompt_groups_a_cu(NB, W) * W / 4)
     const int lo_r = a.window > 0 ? static_cast<int>(max<int64_t>(pos - a.window + 1, 0)) : 0;
     const float c = load_query<KB, NB>(a, (s.first + tok) * a.q.token_stride + (head * group + row - tok * group) * a.q.head_stride, half, q);
     float ref = kNoKey, sum = 0.f;
+    bool far = false;  // a reference of the wave passed kLargeRef
 #pragma unroll
     for (int x = 0; x < NB; ++x) {
 #pragma unroll
@@ -420,6 +421,7 @@ __global__ __launch_bounds__(64 * W, kv_plan::prompt_groups_a_cu(NB, W) * W / 4)
             }
             __builtin_amdgcn_sched_barrier(0);
         };
+        float by = c, less = 0.f;  // the exponent of a weight is its score times by, less this
         // masks, and a reference that the step's scores fit; the weights of
         // `made` steps before it in this tile move with it
         auto settle = [&](int n, int made) {
@@ -454,6 +456,7 @@ __global__ __launch_bounds__(64 * W, kv_plan::prompt_groups_a_cu(NB, W) * W / 4)
                 const float best = fmaxf(ref, ceilf(fmaxf(mark, __shfl_xor(mark, 32))) - kLift);
                 const float z = __builtin_amdgcn_exp2f(ref - best);
                 ref = best;
+                far |= __any(best > kLargeRef || (best < -kLargeRef && best != kNoKey));
                 sum *= z;
 #pragma unroll
                 for (int x = 0; x < NB; ++x) acc[x] *= z;
@@ -463,6 +466,14 @@ __global__ __launch_bounds__(64 * W, kv_plan::prompt_groups_a_cu(NB, W) * W / 4)
                     for (int i = 0; i < 8; ++i) p[u][i] = static_cast<_Float16>(static_cast<float>(p[u][i]) * z);
                 }
             }
+            by = c;
+            less = ref;
+            if (far) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sc[n][i] = sc[n][i] * c - ref;
+                by = 1.f;
+                less = 0.f;
+            }
         };
         // weights of scores 2i and 2i + 1 of step n as the second product
         // takes them: keys r and r + 2 of a run of four
@@ -470,7 +481,7 @@ __global__ __launch_bounds__(64 * W, kv_plan::prompt_groups_a_cu(NB, W) * W / 4)
             const int at = i / 2 * 4 + i % 2;
             h2 w;
 #pragma unroll
-            for (int z = 0; z < 2; ++z) w[z] = static_cast<_Float16>(__builtin_amdgcn_exp2f(fmaf(sc[n][at + 2 * z], c, -ref)));
+            for (int z = 0; z < 2; ++z) w[z] = static_cast<_Float16>(__builtin_amdgcn_exp2f(fmaf(sc[n][at + 2 * z], by, -less)));
             // pinned here: left to itself the compiler moves this to where the
             // weights are used, out from between the products
             w = as_h2(static_cast<uint32_t>(fresh(static_cast<int>(__builtin_bit_cast(uint32_t, w)))));

@@ -190,3 +190,25 @@ def test_hidden_bytes_change_no_bit(dim, news, window, dtype):
             codes[at] = rng.integers(-7, 8, size=(int(at.sum()), dim))
         cache.upload()
         assert torch.equal(prompt(cache, table, lens, news, q, window)[0], clean), fill
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("news", [[1, 1], [9, 5], [300, 280]])
+def test_queries_near_the_types_largest(news, dtype):
+    """Scores of 10^37: the key with the largest takes all of its row, and nothing overflows."""
+    rng = np.random.default_rng(7)
+    lens, page, dim = [330, 290], 32, 64
+    table, pages = layout(rng, page, lens)
+    cache = Cache(rng, pages, HEADS, page, dim, 8, 8)
+    q, q64 = queries(rng, sum(news), dim, DTYPES[dtype], 1e36)
+    starts = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+    note("kv large queries", news, dtype)
+    out = qbd.kv_attention(q, *cache.planes, gpu(table), gpu(np.array(lens, dtype=np.int32)), q_starts=gpu(starts), max_q=max(news),
+                           max_len=32768).double().cpu().numpy()
+    ref, _, _ = kv.attention(q64, cache.k, cache.v, table, lens, starts)
+    assert np.isfinite(out).all()
+    # two keys whose scores are closer than the factors' 11 bits may change places: that is a few rows in a thousand; the
+    # values' own roundings are the output's, and for prompts the 11 bits of V
+    unit = {"f32": 2.0 ** -22, "bf16": 2.0 ** -8 + 2.0 ** -11}[dtype]
+    other = (np.abs(out - ref) > unit * np.abs(ref) + 1e-30).any(-1)
+    assert other.mean() < 0.02, other.mean()
