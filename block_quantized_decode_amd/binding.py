@@ -414,7 +414,8 @@ def kv_cache_read(kc, kd, vc, vd, slots, dtype=torch.float32, k=None, v=None):
 def kv_attention(q, kc, kd, vc, vd, table, lens, q_starts=None, max_q=None, max_len=None, causal=True, window=0,
                  scale=None, out=None, work=None):
     """Attention of the query rows q [T][qheads][dim] over the cached sequences: table int32 [batch][width] of page
-    numbers, lens int32 [batch] (the new tokens among them), q_starts int32 [batch + 1] (None: T / batch rows each).
+    numbers, lens int32 [batch] (the new tokens among them), q_starts int32 [batch + 1] (None: T / batch rows each; rows
+    that it gives to no sequence are not written: pass out where they are to hold something).
     max_q and max_len bound a sequence's rows and length, if known on the host: they shape the launch.  scale is
     1 / sqrt(dim) by default.  work: a uint8 scratch tensor (allocated when None)."""
     c = _kv(kc, kd, vc, vd)

@@ -24,7 +24,8 @@
  * Conventions (every compute entry point)
  *   - Pointers are device pointers (HBM) unless stated otherwise; the caller
  *     owns every buffer.  Inputs are only read; outputs are fully
- *     overwritten, never accumulated into.  The library allocates no memory
+ *     overwritten (kv_attention: the rows of its sequences), never
+ *     accumulated into.  The library allocates no memory
  *     and keeps no workspace: fused entry points write no temporary, and
  *     kv_attention takes scratch memory from the caller.
  *   - Arguments are validated on the host before any HIP call.  The call
@@ -266,7 +267,8 @@ int kv_cache_read(const qbd_kv_cache* cache, const int64_t* slots, int64_t T, in
  * over the keys t < lens[b] that the row sees.  The rows of sequence b are
  * the tokens q_starts[b] .. q_starts[b + 1] - 1 of q [T][qheads][dim]
  * (q_starts NULL: T is a multiple of batch and every sequence has T / batch
- * rows); query head j reads cached head j / (qheads / heads).  The rows are
+ * rows; a row that q_starts gives to no sequence is not written: out keeps
+ * what it held there); query head j reads cached head j / (qheads / heads).  The rows are
  * the last tokens of the sequence: row i of n stands at position
  * lens[b] - n + i.  With causal != 0 it sees the keys at or before its
  * position, and with window > 0 only the last `window` of them; with
