@@ -25,9 +25,9 @@
  *   - Pointers are device pointers (HBM) unless stated otherwise; the caller
  *     owns every buffer.  Inputs are only read; outputs are fully
  *     overwritten (kv_attention: the rows of its sequences), never
- *     accumulated into.  The library allocates no memory
- *     and keeps no workspace: fused entry points write no temporary, and
- *     kv_attention takes scratch memory from the caller.
+ *     accumulated into.  The library allocates no memory and keeps no
+ *     workspace: fused entry points write no temporary, and kv_attention
+ *     takes scratch memory from the caller.
  *   - Arguments are validated on the host before any HIP call.  The call
  *     then enqueues its kernels on `stream` (NULL = the default stream) and
  *     returns without waiting; faults inside a kernel surface at the
