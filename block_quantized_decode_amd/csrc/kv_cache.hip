@@ -14,8 +14,9 @@
 // V's piece, all its loads are under way before the first is used, and 16-bit
 // rows move in 16 bytes.  32768 rows of 8 heads of 128, 4 bits to bf16 (172
 // MB): 42 us, 4.1 TB/s, where K or V a lane and 8-byte accesses took 64; 8190
-// such rows in bf16 into 8 and 4 bits: 16.7 us where they took 18.4.  1, 2 and
-// 4 pieces a lane when reading were level to 4%, 2 when writing 4% slower.
+// such rows in bf16 into 8 and 4 bits: 16.7 us where they took 18.4 (both with
+// the rows in cache; 18.1 from memory).  1, 2 and 4 pieces a lane when reading
+// were level to 4%, 2 when writing 4% slower.
 #include "kv_device.hpp"
 
 namespace qbd {

@@ -30,9 +30,9 @@ constexpr bool bits_ok(int k, int v) { return (k == 4 && v == 4) || (k == 8 && v
 // - more: all items in a row, each with kItemCost tiles of overhead before
 //   its own, are cut into equal shares of at least kMinShare tiles.
 // Measured, us, one query row of four heads a cached head, 8 cached heads of
-// 128 elements in 4 bits, sequences x keys: parts of 1, 4, 16 tiles 14.4,
-// 12.2, 14.8 (1 x 2000) and 16.1, 16.0, 15.4 (8 x 1500); a cost of 0, 8, 24
-// tiles 91, 78, 77 (64 x 1 .. 8192) and 52, 27, 26 (64 x 1 .. 1024); shares
+// 128 elements in 4 bits, sequences x keys: parts of 1, 4, 16 tiles 14.2,
+// 11.6, 14.2 (1 x 2000) and 15.5, 15.2, 14.9 (8 x 1500); a cost of 0, 8, 24
+// tiles 134, 80, 83 (64 x 1 .. 8192) and 71, 25, 25 (64 x 1 .. 1024); shares
 // of 4, 16, 64 tiles and more 24, 24, 39 (64 x 1000).
 constexpr int kTile = 32;
 constexpr int kItemCost = 8;
@@ -41,7 +41,8 @@ constexpr int kMinPart = 4;
 
 // Rows of an item: tiles of 16 that a wave keeps at once.  Two were slower
 // throughout, by their registers (8 heads of 128, 4 bits, 8 x 5000 keys, one
-// tile / two: 20 rows 29.7 / 31.3, 40 rows 42.7 / 47.0, 80 rows 57.2 / 71.6).
+// tile / two, as the kernel then was: 20 rows 29.7 / 31.3, 40 rows 42.7 / 47.0,
+// 80 rows 57.2 / 71.6).
 constexpr int kRowTiles = 1;
 
 // Workgroups of four waves that a CU holds, by the registers of a wave: its
@@ -91,11 +92,11 @@ constexpr double split_items(int heads, int qheads, int64_t batch, int64_t T, in
 }
 
 // Short sequences, and longer ones where they are many: one workgroup an item
-// with no second launch.  Measured as above, so / split: 1 x 500 9.6 / 12.0,
-// 64 x 500 13.6 / 18.3; 1 x 1000 13.4 / 12.1, 8 x 1000 13.6 / 15.8, 64 x
-// 1 .. 1000 17.6 / 26.5; 16 x 2000 22.0 / 19.8, 32 x 2000 22.4 / 25.2, 128 x
-// 1 .. 2000 44.8 / 58.8; 64 x 1 .. 4000 51.0 / 49.0.  Heads of 256 elements
-// (4 cached, 8- and 4-bit): 16 x 1000 21.2 / 17.3, 64 x 1000 22.9 / 27.0.
+// with no second launch.  Measured as above, so / split: 1 x 500 8.9 / 11.4,
+// 64 x 500 13.7 / 17.1; 1 x 1000 12.3 / 11.4, 8 x 1000 12.8 / 14.7, 64 x
+// 1 .. 1000 16.9 / 25.0; 16 x 2000 20.7 / 19.0, 32 x 2000 21.4 / 24.8, 128 x
+// 1 .. 2000 39.6 / 47.2; 64 x 1 .. 4000 43.8 / 42.3.  Heads of 256 elements
+// (4 cached, 8- and 4-bit): 16 x 1000 19.4 / 16.0, 64 x 1000 22.1 / 26.0.
 constexpr bool direct(int dim, int64_t keys, double items, int64_t batch) {
     return keys > 0 && batch <= 65535 && (keys <= 512 || (keys <= 1024 && items >= (dim > 128 ? 256 : 64)) || (keys <= 2048 && items >= 256));
 }
@@ -122,13 +123,14 @@ QBD_HD constexpr int prompt_groups_a_cu(int nb, int waves) {
 // full tiles of rows, the split kernel's time grows with rows x keys from the
 // first.  Measured, this one / the split kernel, 4-bit codes of 128 elements,
 // rows x cached heads of all sequences:
-//    8192 keys    64 x 32  54 / 39    96 x 32  56 / 61    512 x 8  61 / 61    4096 x 8  177 / 417
-//    2048 keys   512 x 8   39 / 23  1024 x 8   44 / 33    256 x 32 43 / 33     512 x 32  49 / 59
-//     512 keys  2048 x 8   32 / 29   512 x 32  33 / 27   1024 x 32 34 / 49
-//   16384 keys   256 x 8   80 / 61    96 x 32  86 / 108   512 x 8  79 / 108
+//    8192 keys    64 x 32  56 / 41    96 x 32  56 / 63    512 x 8  60 / 62    4096 x 8  171 / 404
+//    2048 keys   512 x 8   37 / 21  1024 x 8   41 / 32    256 x 32 43 / 32     512 x 32  47 / 58
+//     512 keys  2048 x 8   32 / 25   512 x 32  33 / 24   1024 x 32 32 / 44
+//   16384 keys   256 x 8   79 / 61    96 x 32  82 / 105   512 x 8  77 / 106
 // so it takes over where rows x heads x (keys + 1300) pass 40 million, and
-// near that for the other sizes and codes (256 elements, 2048 keys: 1024 x 8
-// 73 / 69; 64 elements, 8-bit, 8192 keys: 512 x 8 39 / 42).  A length that the
+// near that for the other sizes and codes (256 elements: 1024 x 8 over 2048
+// keys 65 / 65, 512 x 8 over 8192 103 / 108; 192 elements: 1024 x 8 over 2048
+// 52 / 43; 64 elements, 8-bit: 512 x 8 over 8192 38 / 42).  A length that the
 // host does not know counts as 16384 keys; a window as its keys and the rows',
 // but never as more than the length would without it, so that the workspace,
 // whose size is asked without the window, holds whatever it chooses.
