@@ -15,15 +15,20 @@ typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
 constexpr float kNoKey = -3e38f;  // reference of a row that has seen no key
-// Beyond this a reference and the scores near it are rounded by more than a
-// fused multiply-add's own rounding may differ from them: once a row's reference
-// is there, its wave finds the weights' exponents from rounded products.
-constexpr float kLargeRef = 1048576.f;
 // A product of a weight and a V scale enters the matrix cores in binary16.
 // The reference puts the largest at 2^kLift, and it may grow to 2^kTop
 // before the reference moves: near the top of the type's range, so that
 // weights far below the largest keep their bits (11 down to 2^-28 of it).
 constexpr float kLift = 12.f, kTop = 15.f;
+
+// Scores this large (in log2) are rounded to units of a half and more: neither
+// kLift and kTop nor the residue of a fused product fit between two of them.  A
+// row whose largest is beyond takes it as its reference, as it is, and moves it
+// whenever it grows, and its wave finds the weights' exponents from rounded
+// products: the largest weight is 1 (so weights times V scales below 2^-14 lose
+// bits there).
+constexpr float kFar = 4194304.f;
+__device__ __forceinline__ bool is_far(float score) { return fabsf(score) > kFar && score > kNoKey; }
 
 // A query row enters scaled by a power of two to a maximum of 2^14 or more,
 // below 2^15, so that its elements keep a binary16 number's 11 bits down to

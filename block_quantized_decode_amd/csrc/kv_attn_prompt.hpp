@@ -184,7 +184,7 @@ __global__ __launch_bounds__(64 * W, kv_plan::prompt_groups_a_cu(NB, W) * W / 4)
     const int lo_r = a.window > 0 ? static_cast<int>(max<int64_t>(pos - a.window + 1, 0)) : 0;
     const float c = load_query<KB, NB>(a, (s.first + tok) * a.q.token_stride + (head * group + row - tok * group) * a.q.head_stride, half, q);
     float ref = kNoKey, sum = 0.f;
-    bool far = false;  // a reference of the wave passed kLargeRef
+    bool far = false;  // a reference of the wave is
 #pragma unroll
     for (int x = 0; x < NB; ++x) {
 #pragma unroll
@@ -452,11 +452,13 @@ __global__ __launch_bounds__(64 * W, kv_plan::prompt_groups_a_cu(NB, W) * W / 4)
 #pragma unroll
             for (int i = 1; i < 16; ++i) top = fmaxf(top, sc[n][i]);
             const float mark = top * c;
-            if (__any(mark > ref + kTop)) {
-                const float best = fmaxf(ref, ceilf(fmaxf(mark, __shfl_xor(mark, 32))) - kLift);
+            by = c;
+            less = ref;
+            if (__any(mark > ref + kTop) || far) {
+                const float score = fmaxf(mark, __shfl_xor(mark, 32));
+                const float best = fmaxf(ref, is_far(score) ? score : ceilf(score) - kLift);
                 const float z = __builtin_amdgcn_exp2f(ref - best);
-                ref = best;
-                far |= __any(best > kLargeRef || (best < -kLargeRef && best != kNoKey));
+                ref = less = best;
                 sum *= z;
 #pragma unroll
                 for (int x = 0; x < NB; ++x) acc[x] *= z;
@@ -465,14 +467,13 @@ __global__ __launch_bounds__(64 * W, kv_plan::prompt_groups_a_cu(NB, W) * W / 4)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) p[u][i] = static_cast<_Float16>(static_cast<float>(p[u][i]) * z);
                 }
-            }
-            by = c;
-            less = ref;
-            if (far) {
+                far |= __any(is_far(best));
+                if (far) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) sc[n][i] = sc[n][i] * c - ref;
-                by = 1.f;
-                less = 0.f;
+                    for (int i = 0; i < 16; ++i) sc[n][i] = sc[n][i] * by - less;
+                    by = 1.f;
+                    less = 0.f;
+                }
             }
         };
         // weights of scores 2i and 2i + 1 of step n as the second product

@@ -369,7 +369,7 @@ __global__ __launch_bounds__(256, kv_plan::split_groups_a_cu(KB, VB, NB, RT)) vo
             float ref[RT], sum[RT];
             f4 acc[RT][NB][2];
             int lo_r[RT], hi_r[RT];  // keys that the lane's row sees
-            bool far = false;        // a reference passed kLargeRef
+            bool far = false;        // a reference of the wave is
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 const int row = row0 + min(16 * r + m, rows - 1);
@@ -492,27 +492,29 @@ __global__ __launch_bounds__(256, kv_plan::split_groups_a_cu(KB, VB, NB, RT)) vo
                     float top = sc[r][0];
 #pragma unroll
                     for (int j = 1; j < 8; ++j) top = fmaxf(top, sc[r][j]);
-                    const float mark = top * q[r].c + lb;
-                    if (__any(mark > ref[r] + kTop)) {
-                        float best = fmaxf(mark, __shfl_xor(mark, 16));
-                        best = fmaxf(best, __shfl_xor(best, 32));
-                        best = fmaxf(ref[r], best - kLift);
+                    const float mark = fmaf(top, q[r].c, lb);
+                    float by = q[r].c, less = ref[r];
+                    if (__any(mark > ref[r] + kTop) || far) {
+                        float best = fmaxf(mark, __shfl_xor(mark, 16)), score = top * q[r].c;
+                        best = fmaxf(best, __shfl_xor(best, 32)) - kLift;
+                        score = fmaxf(score, __shfl_xor(score, 16));
+                        score = fmaxf(score, __shfl_xor(score, 32));
+                        best = fmaxf(ref[r], is_far(score) ? score : best);
                         const float f = __builtin_amdgcn_exp2f(ref[r] - best);
-                        ref[r] = best;
-                        far |= __any(best > kLargeRef || (best < -kLargeRef && best != kNoKey));
+                        ref[r] = less = best;
                         sum[r] *= f;
 #pragma unroll
                         for (int y = 0; y < NB; ++y) {
                             acc[r][y][0] *= f;
                             acc[r][y][1] *= f;
                         }
-                    }
-                    float by = q[r].c, less = ref[r];
-                    if (far) {
+                        far |= __any(is_far(best));
+                        if (far) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) sc[r][j] = sc[r][j] * by - less;
-                        by = 1.f;
-                        less = 0.f;
+                            for (int j = 0; j < 8; ++j) sc[r][j] = sc[r][j] * by - less;
+                            by = 1.f;
+                            less = 0.f;
+                        }
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) sc[r][j] = __builtin_amdgcn_exp2f(fmaf(sc[r][j], by, -less));

@@ -212,3 +212,30 @@ def test_queries_near_the_types_largest(news, dtype):
     unit = {"f32": 2.0 ** -22, "bf16": 2.0 ** -8 + 2.0 ** -11}[dtype]
     other = (np.abs(out - ref) > unit * np.abs(ref) + 1e-30).any(-1)
     assert other.mean() < 0.02, other.mean()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("vscale", [(0.02, 0.3), (1e-6, 4e-5), (1000.0, 8000.0)])
+@pytest.mark.parametrize("news", [[1, 1], [300, 280]])
+def test_large_scores_of_every_size(news, vscale, dtype):
+    """Scores of 10^6 to 10^11, where a reference is rounded to units of less than one up to many thousands: finite, and the
+    key with the largest takes all of its row."""
+    rng = np.random.default_rng(8)
+    lens, page, dim = [330, 290], 32, 64
+    table, pages = layout(rng, page, lens)
+    cache = Cache(rng, pages, HEADS, page, dim, 8, 8, vscale=vscale)
+    starts = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+    q0 = rng.standard_normal((sum(news), HEADS * GROUP, dim))
+    for spread in (1e6, 5e6, 1e7, 3e7, 6e7, 1e8, 1.5e8, 2e8, 3e8, 4e8, 6e8, 1e9, 1e11):
+        q = torch.from_numpy((q0 * spread).astype(np.float32)).to(device()).to(DTYPES[dtype])
+        note("kv large scores", news, vscale, dtype, spread)
+        out = qbd.kv_attention(q, *cache.planes, gpu(table), gpu(np.array(lens, dtype=np.int32)), q_starts=gpu(starts), max_q=max(news),
+                               max_len=32768).double().cpu().numpy()
+        ref, _, _ = kv.attention(q.double().cpu().numpy(), cache.k, cache.v, table, lens, starts)
+        assert np.isfinite(out).all(), spread
+        # as above: values by their own roundings, but for a few rows whose two largest scores are closer than the factors' bits;
+        # 16-bit rows' weights times small V scales (below 2^-14 a binary16 product has a fixed step) by 2^-25 of 127
+        unit = {"f32": 2.0 ** -22, "bf16": 2.0 ** -8 + 2.0 ** -11}[dtype]
+        step = {"f32": 1e-30, "bf16": 127 * 2.0 ** -25}[dtype]
+        other = (np.abs(out - ref) > unit * np.abs(ref) + step).any(-1)
+        assert other.mean() < 0.02, (spread, other.mean())
