@@ -19,7 +19,7 @@
 // where there are rows for them (half the expansion of four: 197 -> 185 us at
 // 4096 rows x 8 heads of 8192 keys of 128 elements, 4-bit codes), addresses
 // found for 16 tiles at once and the scales looked at by one wave for all
-// (185 -> 172 us; now 168, 764 TFLOP/s, 58% of what a large fp16 matrix product
+// (185 -> 172 us; now 167, 774 TFLOP/s, 59% of what a large fp16 matrix product
 // reaches), and an order laid out by hand:
 //   scores of keys 0-31        | the next tile's expansion
 //   scores of keys 32-63       | weights of keys 0-31

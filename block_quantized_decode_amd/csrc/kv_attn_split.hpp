@@ -34,13 +34,13 @@
 // rescale nothing.
 //
 // Bound by memory over long histories: 131001 keys of 8 heads of 128 in 4 bits
-// (151 MB) take 40.6 us with the join; by the slope over the length (65536 to
+// (151 MB) take 40.7 us with the join; by the slope over the length (65536 to
 // 262144 keys, cold) it reads 4.8 to 5.2 TB/s, where a plain read reaches 6.0,
 // on a fixed 13 us (the start of a workgroup: lengths, table, queries, first
 // tile; the join's launch).  64 sequences of up to 8192 keys (73 MB) take 30
-// us, 24 with a window of 2048 and heads of 256 (82 MB) 27.7 us.  fp32 rows
+// us, 24 with a window of 2048 and heads of 256 (82 MB) 28.1 us.  fp32 rows
 // are bound by the vector work of their exact splits: four prompts of up to
-// 997 tokens, 14 over 2 heads of 64, 51.8 us.  A sequence's items all walk the
+// 997 tokens, 14 over 2 heads of 64, 52.2 us.  A sequence's items all walk the
 // same keys: those after a causal row tile's last row or before its first row's
 // window are computed and masked, about half of the tiles of such prompts.
 #pragma once
